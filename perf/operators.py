@@ -241,7 +241,7 @@ def _plain_quantize(fmt, x, scale):
         return (x / s32).clamp(-448, 448).to(torch.float8_e4m3fn), None
     if fmt == "q8_0":
         x = x.unflatten(-1, (-1, 32))
-        d = (x.abs().amax(-1, keepdim=True) / torch.full_like(s32, 127.0)).clamp(max=515.5).half()
+        d = (x.abs().amax(-1, keepdim=True) / torch.full_like(s32, 127.0)).clamp(max=65504).half()
         q = torch.where(d == 0, 0, (x / d.float()).round().clamp(-127, 127))
         return q.flatten(-2).to(torch.int8), d.squeeze(-1)
     x = x.unflatten(-1, (-1, 16))
@@ -394,7 +394,7 @@ def _stored(fmt, x, scale):
         return _nearest(_quotient(x, s), _small_floats(4, 3, 448)) * s
     if fmt == "q8_0":
         x = x.unflatten(-1, (-1, 32))
-        d = _quotient(x.abs().amax(-1, keepdim=True), 127.0).half().clamp(max=515.5).double()
+        d = _quotient(x.abs().amax(-1, keepdim=True), 127.0).clamp(max=65504).half().double()
         q = torch.round(_quotient(x, d)).clamp(-127, 127)
         return torch.where(d == 0, 0.0, q * d).flatten(-2)
     x = x.unflatten(-1, (-1, 16))
