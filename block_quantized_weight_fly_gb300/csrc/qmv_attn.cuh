@@ -2,6 +2,7 @@
 // read on the device, barrier and copy primitives, 16-bit operand decoding.
 #pragma once
 #include "qmv_internal.h"
+#include "qmv_attn_geom.h"
 
 namespace qmv {
 
@@ -146,8 +147,7 @@ __device__ __forceinline__ bool seq_info(const AttnArgs& a, int b, SeqInfo* s, b
 }
 // first key that any query of the sequence sees
 __device__ __forceinline__ int seq_first(const AttnArgs& a, const SeqInfo& s) {
-  const int f = a.window ? s.n - s.c - a.window + 1 : 0;
-  return f > 0 ? f : 0;
+  return window_first(s.n - s.c, a.window);
 }
 __device__ __forceinline__ int checked_page(const AttnArgs& a, int page) {
   if (page < 0 || page >= a.c.pages) {

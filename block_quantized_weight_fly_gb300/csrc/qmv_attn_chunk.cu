@@ -189,15 +189,10 @@ struct Unit {
 template <int KT, int QB>
 __device__ __forceinline__ void unit_range(const AttnArgs& a, const SeqInfo& s, int G, int qb, int* tile0, int* nt,
                                            int* last) {
-  const int R = s.c * G;
-  const int r1 = (qb + 1) * QB < R ? (qb + 1) * QB : R;
-  const int p0 = s.n - s.c + qb * QB / G, p1 = s.n - s.c + (r1 - 1) / G;
-  const int hi = a.causal ? p1 : s.n - 1;
-  int lo = a.window ? p0 - a.window + 1 : 0;
-  if (lo < 0) lo = 0;
-  *tile0 = lo / KT;
-  *nt = hi < lo ? 0 : hi / KT - lo / KT + 1;
-  *last = hi;
+  const BlockRange r = block_range<KT, QB>(s.n, s.c, G, qb, a.causal, a.window);
+  *tile0 = r.tile0;
+  *nt = r.nt;
+  *last = r.last;
 }
 // what a block of rows adds to the numbered tiles
 template <int KT, int QB>
@@ -251,12 +246,10 @@ struct Full {
 };
 template <int QB>
 __device__ __forceinline__ Full unit_full(const AttnArgs& a, const Unit& u, int G) {
-  const int R = u.s.c * G;
-  const int r1 = (u.qb + 1) * QB < R ? (u.qb + 1) * QB : R;
-  const int p0 = u.s.n - u.s.c + u.qb * QB / G, p1 = u.s.n - u.s.c + (r1 - 1) / G;
+  const BlockRange r = block_range<kSub, QB>(u.s.n, u.s.c, G, u.qb, a.causal, a.window);
   Full f;
-  f.hi = a.causal ? p0 : u.s.n - 1;
-  f.lo = a.window ? p1 - a.window + 1 : 0;
+  f.hi = a.causal ? r.first_pos : u.s.n - 1;
+  f.lo = window_first(r.last_pos, a.window);
   return f;
 }
 
@@ -890,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
         const float rf = rf_next;
         const int pos = u.s.n - u.s.c + tok;
         const int see_hi = a.causal ? pos : u.s.n - 1;          // first and last key that this row sees
-        const int see_lo = a.window ? pos - a.window + 1 : 0;
+        const int see_lo = window_first(pos, a.window);
         const Full full = unit_full<QB>(a, u, G);
         float m = -INFINITY, l = 0.0f;
         bool bad_row = false;

@@ -1,0 +1,41 @@
+// qmv_attn_geom.h -- which keys a query, or a block of query rows, sees, and the tiles they
+// make: integer arithmetic alone, so that a host compiler can build it for tests too.
+//
+// A sequence has n cached tokens, the last c of them new; its query i stands at position
+// n - c + i, which is negative for the first ones when c > n. window is 0 (none) or any
+// positive int.
+#pragma once
+#include <cstdint>
+
+#ifdef __CUDACC__
+#define QMV_HD __host__ __device__ __forceinline__
+#else
+#define QMV_HD inline
+#endif
+
+namespace qmv {
+
+// first key that the query at position pos sees. pos - window is formed only where it
+// cannot leave 32 bits: window may be the largest int, and pos negative.
+QMV_HD int window_first(int pos, int window) { return window == 0 || pos < window ? 0 : pos - window + 1; }
+
+// Rows qb QB .. (qb + 1) QB - 1 of a sequence (row = token * G + query head), as far as it has them
+struct BlockRange {
+  int first_pos, last_pos;   // positions of its first and last token
+  int tile0, nt, last;       // first key tile of KT tokens, key tiles, last key that a row sees
+};
+template <int KT, int QB>
+QMV_HD BlockRange block_range(int n, int c, int G, int qb, bool causal, int window) {
+  const int R = c * G;
+  const int r1 = (qb + 1) * QB < R ? (qb + 1) * QB : R;
+  BlockRange b;
+  b.first_pos = n - c + qb * QB / G;
+  b.last_pos = n - c + (r1 - 1) / G;
+  b.last = causal ? b.last_pos : n - 1;
+  const int lo = window_first(b.first_pos, window);
+  b.tile0 = lo / KT;
+  b.nt = b.last < lo ? 0 : b.last / KT - lo / KT + 1;
+  return b;
+}
+
+}  // namespace qmv
