@@ -324,6 +324,10 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D, NT>::NW * 32, 1) attn_rows_ker
     per = place_div(total + gridDim.x - 1, gridDim.x);
     const int least = kUnitCost + (longest <= 3 * C::NW ? longest : C::NW);
     if (per < least) per = least;
+    if (per > kMostPlaces) {
+      if (blockIdx.x == 0 && tid == 0) atomicOr(a.status, kStatRange);
+      total = 0;
+    }
     w0 = (int64_t)blockIdx.x * per;
     w1 = w0 + per < total ? w0 + per : total;
   };

@@ -121,6 +121,9 @@ __device__ __forceinline__ void row_scale(float amax, float* mul, float* inv) {
   *inv = __uint_as_float((uint32_t)(254 - f) << 23);
 }
 
+// A CTA's places among the numbered tiles are 32-bit integers from the start of its range; a
+// batch that gives one more than this many (half a minute of work at least) latches QMV_ERANGE instead
+constexpr int64_t kMostPlaces = (int64_t)1 << 30;
 // places among the numbered tiles nearly always fit 32 bits, where a division is a fifth as long
 __device__ __forceinline__ int64_t place_div(int64_t a, int64_t b) {
   return ((a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;

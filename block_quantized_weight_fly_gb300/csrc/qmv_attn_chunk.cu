@@ -194,12 +194,12 @@ __device__ __forceinline__ void unit_range(const AttnArgs& a, const SeqInfo& s, 
   *nt = r.nt;
   *last = r.last;
 }
-// what a block of rows adds to the numbered tiles
+// the numbered tiles of one head's blocks, in every lane of the warp
 template <int KT, int QB>
-__device__ __forceinline__ int unit_cost(const AttnArgs& a, const SeqInfo& s, int G, int qb) {
-  int t0, nt, hi;
-  unit_range<KT, QB>(a, s, G, qb, &t0, &nt, &hi);
-  return nt ? nt + unit_overhead(KT) : 0;
+__device__ __forceinline__ int64_t head_cost(const AttnArgs& a, const SeqInfo& s, int G, int nqb, int lane) {
+  int64_t sum = blocks_cost<KT, QB>(s.n, s.c, G, nqb, lane, a.causal, a.window, unit_overhead(KT));
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
 }
 template <int KT, int QB>
 __device__ __forceinline__ void unit_seq(const AttnArgs& a, Unit& u, int G) {
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
   __shared__ uint32_t s_poison[8][4];                        // per tile (mod 8): its tokens with a non-finite value
   __shared__ uint32_t s_tmem;
   __shared__ int s_last[2];
-  int* const s_sum = reinterpret_cast<int*>(qtile);          // [kThreads], while the work is laid out
+  int64_t* const s_sum = reinterpret_cast<int64_t*>(qtile);  // [kThreads], while the work is laid out
   // barriers
   const uint32_t bar = smem_u32(ctrl);
   const uint32_t raw_full = bar, raw_empty = raw_full + 8 * C::NRAW, op_full = raw_empty + 8 * C::NRAW,
@@ -422,18 +422,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
       const int cnt = a.B - b0 < kThreads ? a.B - b0 : kThreads;
       for (int i = warp; i < kThreads; i += kThreads / 32) {
-        int sum = 0;
+        int64_t sum = 0;
         if (i < cnt) {
           SeqInfo s;
           seq_info(a, b0 + i, &s, pass == 0 && blockIdx.x == 0 && lane == 0);
           const int nqb = s.c * G > a.few_rows ? (s.c * G + QB - 1) / QB : 0;
-          for (int qb = lane; qb < nqb; qb += 32) sum += unit_cost<KT, QB>(a, s, G, qb);
-          for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          sum = head_cost<KT, QB>(a, s, G, nqb, lane);
         }
         if (lane == 0) s_sum[i] = sum;
       }
       __syncthreads();
-      const int64_t mine = (int64_t)s_sum[tid] * a.c.heads;
+      const int64_t mine = s_sum[tid] * a.c.heads;
       int64_t scan = mine;
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
@@ -460,6 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
       total = base;
       per = place_div(total + gridDim.x - 1, gridDim.x);
       if (per < unit_overhead(KT) + 2) per = unit_overhead(KT) + 2;
+      if (per > kMostPlaces) {
+        if (blockIdx.x == 0 && tid == 0) atomicOr(a.status, kStatRange);
+        total = 0;
+      }
       w0 = (int64_t)blockIdx.x * per;
       w1 = w0 + per < total ? w0 + per : total;
     }
@@ -476,18 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
     first.b = (int)s_first[0];
     unit_seq<KT, QB>(a, first, G);
     // head and block: tiles of one head's blocks, in turn
-    int per_head = 0;
-    for (int qb = 0; qb < first.nqb; qb += 32) {
-      int cost = qb + lane < first.nqb ? unit_cost<KT, QB>(a, first.s, G, qb + lane) : 0;
-      for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
-      per_head += cost;
-    }
-    first.h = (int)(s_first[1] / per_head);
-    int rest = (int)(s_first[1] % per_head);
+    const int64_t per_head = head_cost<KT, QB>(a, first.s, G, first.nqb, lane);
+    first.h = (int)place_div(s_first[1], per_head);
+    int64_t rest = s_first[1] - first.h * per_head;
     first.qb = 0;
     for (int qb = 0; qb < first.nqb; qb += 32) {
-      const int cost = qb + lane < first.nqb ? unit_cost<KT, QB>(a, first.s, G, qb + lane) : 0;
-      int scan = cost;
+      const int cost = qb + lane < first.nqb ? block_cost<KT, QB>(first.s.n, first.s.c, G, qb + lane, a.causal, a.window,
+                                                                  unit_overhead(KT)) : 0;
+      int scan = cost;                                           // of 32 blocks: below 2^31
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, scan, o);
         if (lane >= o) scan += v;
@@ -503,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
       rest -= all;
     }
     unit_range<KT, QB>(a, first.s, G, first.qb, &first.tile0, &first.nt, &first.hi);
-    first.org = unit_overhead(KT) - rest;
+    first.org = unit_overhead(KT) - (int)rest;
     first.k = first.org < 0 ? -first.org : 0;
     work = unit_here(first, len);
   }

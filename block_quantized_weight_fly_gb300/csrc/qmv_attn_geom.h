@@ -38,4 +38,20 @@ QMV_HD BlockRange block_range(int n, int c, int G, int qb, bool causal, int wind
   return b;
 }
 
+
+// What a block adds to the numbered tiles: its key tiles and `overhead`; 0 without a key tile
+template <int KT, int QB>
+QMV_HD int block_cost(int n, int c, int G, int qb, bool causal, int window, int overhead) {
+  const int nt = block_range<KT, QB>(n, c, G, qb, causal, window).nt;
+  return nt ? nt + overhead : 0;
+}
+// Blocks lane, lane + 32, ... of a sequence's nqb. A sequence's sum can pass 32 bits: 2^20
+// queries of 16 heads over 2^20 keys are 2^17 blocks of 2^14 tiles.
+template <int KT, int QB>
+QMV_HD int64_t blocks_cost(int n, int c, int G, int nqb, int lane, bool causal, int window, int overhead) {
+  int64_t sum = 0;
+  for (int qb = lane; qb < nqb; qb += 32) sum += block_cost<KT, QB>(n, c, G, qb, causal, window, overhead);
+  return sum;
+}
+
 }  // namespace qmv

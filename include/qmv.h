@@ -452,7 +452,8 @@ size_t qmv_attn_workspace_size(const qmv_kv_cache* cache, int q_heads);
  * no sequence are left unwritten. max_q: an upper bound of c, known to the host, which
  * picks the kernel. A kv_len outside 0 .. max_pages * page_size, a c above max_q, a
  * q_start out of order or a page id outside the cache latches QMV_ERANGE; the
- * sequence's outputs are then unspecified, nothing else is touched. Table entries of
+ * sequence's outputs are then unspecified, nothing else is touched. So does a batch of
+ * more than 2^30 key tiles per SM (half a minute of work at least): none of it is computed. Table entries of
  * pages without a visible token are not followed (behind a window, they may be stale).
  * A batch that mixes single tokens and chunks launches two kernels, others one. Not
  * served: T * q_heads or max_pages * page_size of 2^31 and more, max_q rows per KV head or

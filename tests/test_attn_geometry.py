@@ -20,6 +20,11 @@ extern "C" void range(int wide, int n, int c, int G, int qb, int causal, int win
                             : block_range<128, 256>(n, c, G, qb, causal != 0, window);
   out[0] = b.first_pos; out[1] = b.last_pos; out[2] = b.tile0; out[3] = b.nt; out[4] = b.last;
 }
+extern "C" long long cost(int wide, int n, int c, int G, int lane, int causal, int window, int overhead) {
+  const int nqb = (c * G + (wide ? 127 : 255)) / (wide ? 128 : 256);
+  return wide ? blocks_cost<64, 128>(n, c, G, nqb, lane, causal != 0, window, overhead)
+              : blocks_cost<128, 256>(n, c, G, nqb, lane, causal != 0, window, overhead);
+}
 """
 
 
@@ -28,7 +33,9 @@ def compile_host(tmp, source):
     with open(src, "w") as f:
         f.write(source)
     subprocess.run(["g++", "-std=c++17", "-O1", "-fwrapv", "-shared", "-fPIC", "-I", CSRC, src, "-o", so], check=True)
-    return ctypes.CDLL(so)
+    lib = ctypes.CDLL(so)
+    lib.cost.restype = ctypes.c_longlong
+    return lib
 
 
 @pytest.fixture(scope="module")
@@ -74,3 +81,22 @@ def test_keys_of_a_block_of_rows(geom, wide, KT, QB, causal, n, c):
                 assert got[3] == (0 if hi < lo else hi // KT - lo // KT + 1), (window, G, qb)
                 if got[3]:
                     assert got[2] == lo // KT
+
+
+@pytest.mark.parametrize("wide,KT,QB", [(0, 128, 256), (1, 64, 128)])
+@pytest.mark.parametrize("n,c,G,causal,window", [
+    (1 << 20, 1 << 20, 16, 0, 0),               # past 2^31 with 64-token tiles: 2^17 blocks of 2^14 + 8
+    (3 << 20, 3 << 20, 16, 1, 0),               # a causal triangle past 2^31
+    (1 << 20, 1 << 20, 16, 1, 4096),
+    (700, 300, 5, 1, 0), (3, 300, 4, 1, 7), (0, 9, 2, 0, 0),
+])
+def test_cost_of_a_sequence(geom, wide, KT, QB, n, c, G, causal, window):
+    over, want = 8, 0
+    for qb in range(-(-c * G // QB)):
+        r1 = min((qb + 1) * QB, c * G) - 1
+        lo, hi = first_seen(n - c + qb * QB // G, window), n - c + r1 // G if causal else n - 1
+        want += 0 if hi < lo else hi // KT - lo // KT + 1 + over
+    lanes = [geom.cost(wide, n, c, G, lane, causal, window, over) for lane in range(32)]
+    assert sum(lanes) == want
+    if wide and n >= 1 << 20 and not window:
+        assert want > 2 ** 31
