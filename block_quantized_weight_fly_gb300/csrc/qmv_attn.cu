@@ -259,7 +259,7 @@ struct Cursor {
 template <int TILE>
 __device__ __forceinline__ int unit_tiles(const AttnArgs& a, const SeqInfo& s) {
   if (s.c * (a.q_heads / a.c.heads) > a.few_rows) return 0;
-  return s.n == 0 || s.c == 0 ? 0 : (s.n + TILE - 1) / TILE - seq_first(a, s) / TILE;
+  return s.n == 0 || s.c == 0 ? 0 : tiles_of<TILE>(s.n, seq_first(a, s));
 }
 // move on by `step` tiles; false past the last sequence
 template <int TILE>

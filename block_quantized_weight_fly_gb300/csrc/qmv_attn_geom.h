@@ -19,6 +19,13 @@ namespace qmv {
 // cannot leave 32 bits: window may be the largest int, and pos negative.
 QMV_HD int window_first(int pos, int window) { return window == 0 || pos < window ? 0 : pos - window + 1; }
 
+// tiles of TILE tokens from the one that holds token `first` to the one that holds token n - 1
+// (n > 0, up to 2^31 - 16: n + TILE - 1 may leave 32 bits)
+template <int TILE>
+QMV_HD int tiles_of(int n, int first) {
+  return (n - 1) / TILE + 1 - first / TILE;
+}
+
 // Rows qb QB .. (qb + 1) QB - 1 of a sequence (row = token * G + query head), as far as it has them
 struct BlockRange {
   int first_pos, last_pos;   // positions of its first and last token

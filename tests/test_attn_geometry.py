@@ -20,6 +20,7 @@ extern "C" void range(int wide, int n, int c, int G, int qb, int causal, int win
                             : block_range<128, 256>(n, c, G, qb, causal != 0, window);
   out[0] = b.first_pos; out[1] = b.last_pos; out[2] = b.tile0; out[3] = b.nt; out[4] = b.last;
 }
+extern "C" int tiles(int tile, int n, int first) { return tile == 32 ? tiles_of<32>(n, first) : tiles_of<16>(n, first); }
 extern "C" long long cost(int wide, int n, int c, int G, int lane, int causal, int window, int overhead) {
   const int nqb = (c * G + (wide ? 127 : 255)) / (wide ? 128 : 256);
   return wide ? blocks_cost<64, 128>(n, c, G, nqb, lane, causal != 0, window, overhead)
@@ -100,3 +101,10 @@ def test_cost_of_a_sequence(geom, wide, KT, QB, n, c, G, causal, window):
     assert sum(lanes) == want
     if wide and n >= 1 << 20 and not window:
         assert want > 2 ** 31
+
+
+@pytest.mark.parametrize("tile", [16, 32])
+def test_tiles_of_a_sequence(geom, tile):
+    for n in (1, 15, 16, 17, 31, 32, 33, 1000, 2 ** 31 - 48, 2 ** 31 - 17, 2 ** 31 - 16):
+        for first in {0, n // 2, n - 1}:
+            assert geom.tiles(tile, n, first) == -(-n // tile) - first // tile, (n, first)
