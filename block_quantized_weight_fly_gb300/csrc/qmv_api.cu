@@ -486,6 +486,9 @@ qmv_status kv_geometry(const qmv_kv_cache* d, KvCache* c) {
   while ((1 << c->page_shift) < d->page_size) ++c->page_shift;
   c->heads = d->heads;
   c->dim = d->head_dim;
+  // a page is at most 2^36 bytes; the pages' sum must not leave 64 bits
+  const int64_t page = (int64_t)c->heads * ((int64_t)kv_group_bytes(c->fmt, c->dim) << (c->page_shift - 3));
+  if (d->pages > (((int64_t)1 << 48) - 1) / page) return QMV_EUNSUPPORTED;
   return QMV_OK;
 }
 

@@ -389,7 +389,8 @@ typedef enum {
 } qmv_kv_fmt;
 
 /* One layer's cache: `pages` pages of page_size tokens for `heads` KV heads of head_dim
- * values. page_size: a power of two, 16 .. 1024. head_dim: 64, 128 or 256. data: device,
+ * values, less than 2^48 bytes in all. page_size: a power of two, 16 .. 1024. head_dim: 64,
+ * 128 or 256. heads: up to 65536. pages: below 2^31. data: device,
  * qmv_kv_cache_size bytes, 256-byte aligned, owned by the caller; it needs no
  * initial value. k_scale, v_scale: the static scales of FP8 and NVFP4 (finite, > 0; the
  * other formats ignore them). The layout is the library's own (qmv_kv_read gives the
