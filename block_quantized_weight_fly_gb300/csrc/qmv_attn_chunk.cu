@@ -715,7 +715,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
         uint32_t* poison = s_poison[tileno & 7];
         if constexpr (BF) {
           const int vu = use + 1;
-          ok = bar_wait(op_full + 8 * (vu % C::NOP), (uint32_t)((vu / C::NOP) & 1));
+          // The slot's release first, as the producer waits for it. With five slots its last
+          // occupant was a keys tile, whose arrival no converter has seen: while that copy is under
+          // way, the parity of the phase after it looks like a completed one, and a warp would
+          // run ahead of its tiles, past a phase of op_fix that others have yet to arrive at
+          if (vu >= C::NOP) ok = bar_wait(op_free(vu - C::NOP), op_free_parity(vu - C::NOP));
+          ok = ok && bar_wait(op_full + 8 * (vu % C::NOP), (uint32_t)((vu / C::NOP) & 1));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (edge) {
