@@ -26,7 +26,6 @@ namespace qmv {
 
 namespace {
 
-constexpr int kLazy = 8;               // log2 of the growth of a maximum that O tolerates
 // A unit (one KV head of one sequence) counts as its tiles plus this many: its queries and
 // the join of its parts take about as long, and shares are cut to be equal in time
 constexpr int kUnitCost = 16;
@@ -644,7 +643,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D, NT>::NW * 32, 1) attn_rows_ker
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
           mt[nt][i] = v;
-          grow |= v > m[nt][i] + kLazy;
+          grow |= v > m[nt][i] + (kHead<BF> + kLazy);
         }
       }
       if (__any_sync(0xffffffffu, grow)) {
@@ -652,7 +651,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D, NT>::NW * 32, 1) attn_rows_ker
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float mn = fmaxf(m[nt][i], mt[nt][i]);
+            const float mn = fmaxf(m[nt][i], mt[nt][i] - kHead<BF>);
             const float fac = mn == -INFINITY ? 1.0f : ex2(m[nt][i] - mn);
             m[nt][i] = mn;
             l[nt][i] *= fac;

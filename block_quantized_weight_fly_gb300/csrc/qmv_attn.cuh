@@ -9,6 +9,16 @@ namespace qmv {
 constexpr unsigned long long kAttnTimeoutNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Probabilities are formed against a reference per row, in base 2: p = 2^(s - m). m is raised only
+// when a logit passes it by more than kHead + kLazy, and then to kHead below the largest. f16
+// probabilities use f16's range for the small ones: with kHead = 7 the largest is between 2^7
+// and 2^15, so one that f16's smallest step, 2^-24, rounds off is below 2^-32 of it (2^18 keys
+// beside one that outweighs them by e^18 still count; at kHead = 0 they were lost). bf16 has
+// fp32's range. m stands for the reference wherever parts are joined.
+constexpr int kLazy = 8;               // log2 of the growth of a maximum that O tolerates
+template <bool BF>
+constexpr int kHead = BF ? 0 : 7;
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ unsigned long long attn_timer() {
   unsigned long long t;

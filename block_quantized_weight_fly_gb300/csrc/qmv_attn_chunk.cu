@@ -31,7 +31,6 @@ namespace qmv {
 
 namespace {
 
-constexpr int kLazy = 8;
 constexpr int kThreads = 512;
 constexpr int kSub = 64;               // keys per S tile
 // A unit counts as its key tiles plus this many: its queries, its last product and its
@@ -944,8 +943,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
             for (int q = 0; q < 4; ++q)
               mx[q] = max3(mx[q], __uint_as_float(s[e + 2 * q]), __uint_as_float(s[e + 2 * q + 1]));
           const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * rf;
-          if (__builtin_expect(__any_sync(0xffffffffu, mt > m + kLazy), 0)) {
-            const float mn = fmaxf(m, mt);
+          if (__builtin_expect(__any_sync(0xffffffffu, mt > m + (kHead<BF> + kLazy)), 0)) {
+            const float mn = fmaxf(m, mt - kHead<BF>);
             const float fac = mn == -INFINITY ? 1.0f : ex2(m - mn);
             m = mn;
             l *= fac;

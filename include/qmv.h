@@ -461,7 +461,8 @@ size_t qmv_attn_workspace_size(const qmv_kv_cache* cache, int q_heads);
  * max_pages * page_size / 16 * heads of 2^30 and more.
  * Sums, maxima and the output accumulate in fp32. Keys, values and queries enter the
  * products exactly, Q8_0 ones as f16(d q); probabilities are rounded to 16
- * bits (f16, for a BF16 cache bf16) before they meet the values. */
+ * bits before they meet the values: for a BF16 cache to bf16 (2^-8 of each), else to f16
+ * (2^-11 of each; one below 2^-21 of its row's largest, by up to 2^-32 of the largest). */
 qmv_status qmv_attn_paged(const qmv_kv_cache* cache, const uint16_t* q, int64_t q_token_stride,
                           const int32_t* page_table, int64_t max_pages, const int32_t* kv_len,
                           const int32_t* q_start, int B, int64_t T, int max_q, int q_heads, float scale,
