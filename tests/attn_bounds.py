@@ -27,3 +27,13 @@ def tight(fmt, out, lse, mag, dots, n, vmax):
     b = mag * rel[..., None] + small
     b = b + 2.0 ** -8 * (out.abs() + b) + 1e-38
     return b, logit + sums + 2.0 ** -22 * lse.abs().nan_to_num(0, 0, 0) + 1e-6
+
+
+def drift(n, heads, dim, g, device="cpu"):
+    """Value means [n, heads, dim] of size 3 that turn once along the sequence, each channel at a
+    phase of its own: their sum over the whole sequence is near zero, over any contiguous
+    part it is not in some channel, so an output that misses, doubles or misweights a part is
+    off by about three times the part's softmax weight."""
+    phase = 6.2831853 * torch.rand((1, heads, dim), generator=g, device=device)
+    turn = 6.2831853 * torch.arange(n, device=device)[:, None, None] / n
+    return 3 * torch.cos(turn + phase)

@@ -1,12 +1,14 @@
-"""Paged attention over contexts near the longest it takes."""
+"""Paged attention over long contexts, held to bounds that see a lost part, and over contexts near
+the longest it takes."""
 import math
 
 import pytest
 import torch
 
+import attn_bounds
 import kv_ref
-from test_gpu_attn import q  # noqa: F401 (fixture)
-from test_gpu_kv_cache import SCALE
+from test_gpu_attn import Batch, q  # noqa: F401 (fixture)
+from test_gpu_kv_cache import FMTS, SCALE
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +37,25 @@ def test_contexts_up_to_2_31(q, n, c, causal):  # noqa: F811
     sums = 16 * (2 ** 24 / 152) * 2.0 ** -24 + 2.0 ** -9
     assert ((out.double() - ref).abs() <= sums * mag + 2.0 ** -7 * (mag + ref.abs())).all()
     assert ((lse.double() - rl - math.log(n / page)).abs() <= 2 * sums).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[(1, 40000), (1, 3)], [(8, 20011)], [(4, 30011), (3, 9000)], [(130, 9000), (1, 20000)],
+                                  [(64, 60000)]])
+def test_no_part_of_a_long_context_is_lost(q, fmt, D, lens):  # noqa: F811
+    def edit(b, k, v):
+        g = torch.Generator(device="cuda").manual_seed(43)
+        for s, (_, n) in zip(b.slots, b.lens):
+            v[s.cuda()] = (0.5 * v[s.cuda()] + attn_bounds.drift(n, 1, D, g, "cuda")).bfloat16()
+    b = Batch(q, fmt, 4, 1, D, 64, lens, seed=42, edit=edit)
+    out, lse = b.run(q)
+    sc = float(torch.tensor(D ** -0.5))
+    t = 0
+    for (c, n), k, v in zip(lens, b.keys, b.values):
+        rows = slice(t, t + c)
+        ref, rl, mag, dots = kv_ref.attention(b.q[rows].double(), [k], [v], [(c, n)], sc, True, 0)
+        bo, bl = attn_bounds.tight(fmt, ref, rl, mag, dots, n, float(v.abs().max()))
+        assert ((out[rows].double() - ref).abs() <= bo).all()
+        assert ((lse[rows].double() - rl).abs() <= bl).all()
+        t += c
