@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
   const uint32_t raw_full = bar, raw_empty = raw_full + 8 * C::NRAW, op_full = raw_empty + 8 * C::NRAW,
                  op_done = op_full + 8 * C::NOP, op_fix = op_done + 64, q_ready = op_fix + 32,
                  s_full = q_ready + 16, p_ready = s_full + 32, o_done = p_ready + 32, joined = o_done + 16,
-                 all_done = joined + 16;
+                 all_done = joined + 16, marked = all_done + 8;
   // s_full, p_ready: [row tile][S buffer]. op_done: [keys, values][tile % 4], the products of
   // a tile are complete: a slot's last occupant may be of the other kind, so its release is
   // told by tile, and no waiter is four tiles from a barrier's phase
@@ -405,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
       bar_init(op_done + 32 + 8 * i, 1);
     }
     bar_init(all_done, 1);
+    bar_init(marked, 4);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (tid < 32) s_poison[tid >> 2][tid & 3] = 0u;
@@ -790,7 +791,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
     constexpr int PP = D / 8, RPI = 32 / PP == 0 ? 1 : 32 / PP;          // pieces per row, rows per instruction
     uint8_t* const wtile = qtile + w * C::QT + (warp & 3) * 4 * C::GRP;  // this warp's 32 rows of the query tile
     Unit u = first;
-    uint32_t n_even = 0, n_odd = 0, nd = 0, nj = 0;   // phases of the two S barriers, O, joins
+    uint32_t n_even = 0, n_odd = 0, nd = 0, nj = 0, nm = 0;   // phases of the two S barriers, O, joins, marks
+    bool marks_due = false;
     uint32_t tileno = 0;
     bool ok = true;
     // The queries of a unit's 32 rows into the operand tile (free once the last S of the unit
@@ -879,6 +881,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
         unit_next<KT, QB>(a, un, G);
         if (active(un)) prefetch(un);
       }
+      // Behind a unit with two row tiles, one with a single tile goes on without the second tile's
+      // warps: its first probabilities wait until those have read the marks of their last
+      // tiles, which later tiles would write over
+      const bool leaves = pair && after && !(un.s.c * G - un.qb * QB > 128);
+      if (w == 0 && marks_due) {
+        ok = bar_wait(marked, nm & 1u);
+        ++nm;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
+      marks_due = leaves;
       if (w == 0 || pair) {
         const int r = r0 + 128 * w + row;
         const bool real = r < R;
@@ -1021,6 +1034,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
         if (!ok) break;
         tc_after();
         for (int j = ns > 2 ? ns - 2 : 0; j < ns; ++j) marks(j);
+        if (w == 1 && leaves) {
+          __syncwarp();
+          if (lane == 0) bar_arrive(marked);
+        }
         const int64_t ustart = w0 + u.org;
         const int i0 = (int)place_div(ustart, per), i1 = (int)place_div(ustart + u.nt - 1, per);
         const bool whole = i0 == i1;
