@@ -64,6 +64,12 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// The two attention kernels of one call run beside each other: either may start on the SMs that
+// the one before it leaves (let_next_start), and neither ends before it (wait_for_previous,
+// by one thread of every CTA). Both do nothing where a kernel is launched by itself.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- 16-bit operands ------------------------------------------------------------
 __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -185,10 +191,26 @@ __device__ __forceinline__ void zero_unseeing(const AttnArgs& a, int tid, int th
   }
 }
 
-cudaError_t launch_attn_rows(const AttnArgs& a, int sms, cudaStream_t s);
+// A CTA per SM; `second`: it may start before the launch in front of it has ended
+template <typename Params>
+cudaError_t launch_beside(void (*kernel)(Params), const Params& p, int sms, int threads, int smem, bool second,
+                          cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sms);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = second ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+// second: right behind the other one, whose CTAs it may run beside (they share nothing)
+cudaError_t launch_attn_rows(const AttnArgs& a, int sms, bool second, cudaStream_t s);
 int64_t attn_rows_workspace(const KvCache& c, int sms);
-// after_rows: right behind launch_attn_rows, whose CTAs it may run beside (they share nothing)
-cudaError_t launch_attn_chunk(const AttnArgs& a, int sms, bool after_rows, cudaStream_t s);
+cudaError_t launch_attn_chunk(const AttnArgs& a, int sms, bool second, cudaStream_t s);
 int64_t attn_chunk_workspace(const KvCache& c, int sms);
 
 }  // namespace qmv

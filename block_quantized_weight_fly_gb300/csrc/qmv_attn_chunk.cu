@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
   // told by tile, and no waiter is four tiles from a barrier's phase
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.q_heads / a.c.heads;
+  let_next_start();
   // the barrier, and its phase, that frees the slot of use m (K0 V0 K1 V1 ...)
   auto op_free = [&](int m) { return op_done + 32u * (m & 1) + 8u * ((m >> 1) & 3); };
   auto op_free_parity = [](int m) { return (uint32_t)((m >> 3) & 1); };
@@ -1191,13 +1192,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
   }
   tc_before();
   __syncthreads();
-  // launched beside the streaming kernel: this grid ends after that one
-  if (tid == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tid == 0) wait_for_previous();
   if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 template <int FMT, int D>
-cudaError_t chunk_go(const ChunkParams& p, int sms, bool after_rows, cudaStream_t s) {
+cudaError_t chunk_go(const ChunkParams& p, int sms, bool second, cudaStream_t s) {
   using C = ChunkCfg<FMT, D>;
   static_assert(C::NOP >= 3 && (C::BF || C::NRAW >= 2), "rings");
   static_assert(C::SMEM <= 232448 - 512, "shared memory");
@@ -1216,23 +1216,13 @@ cudaError_t chunk_go(const ChunkParams& p, int sms, bool after_rows, cudaStream_
     if (err != cudaSuccess) return err;
     opted[dev] = 1;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)sms);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = after_rows ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_chunk_kernel<FMT, D>, p);
+  return launch_beside(attn_chunk_kernel<FMT, D>, p, sms, kThreads, C::SMEM, second, s);
 }
 template <int FMT>
-cudaError_t chunk_dim(const ChunkParams& p, int sms, bool after_rows, cudaStream_t s) {
-  return p.a.c.dim == 64    ? chunk_go<FMT, 64>(p, sms, after_rows, s)
-         : p.a.c.dim == 128 ? chunk_go<FMT, 128>(p, sms, after_rows, s)
-                            : chunk_go<FMT, 256>(p, sms, after_rows, s);
+cudaError_t chunk_dim(const ChunkParams& p, int sms, bool second, cudaStream_t s) {
+  return p.a.c.dim == 64    ? chunk_go<FMT, 64>(p, sms, second, s)
+         : p.a.c.dim == 128 ? chunk_go<FMT, 128>(p, sms, second, s)
+                            : chunk_go<FMT, 256>(p, sms, second, s);
 }
 
 }  // namespace
@@ -1243,7 +1233,7 @@ int64_t attn_chunk_workspace(const KvCache& c, int sms) {
   return align_up((int64_t)sms * 8, 256) + (int64_t)sms * 2 * rows * (c.dim + 2) * 4;
 }
 
-cudaError_t launch_attn_chunk(const AttnArgs& a, int sms, bool after_rows, cudaStream_t s) {
+cudaError_t launch_attn_chunk(const AttnArgs& a, int sms, bool second, cudaStream_t s) {
   ChunkParams p;
   p.a = a;
   p.a.out_wide = (reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride % 16 == 0) ? 1 : 0;
@@ -1251,10 +1241,10 @@ cudaError_t launch_attn_chunk(const AttnArgs& a, int sms, bool after_rows, cudaS
   p.counters = reinterpret_cast<unsigned*>(ws);
   p.parts = reinterpret_cast<float*>(ws + align_up((int64_t)sms * 8, 256));
   switch (a.c.fmt) {
-    case KV_BF16: return chunk_dim<KV_BF16>(p, sms, after_rows, s);
-    case KV_Q8_0: return chunk_dim<KV_Q8_0>(p, sms, after_rows, s);
-    case KV_FP8: return chunk_dim<KV_FP8>(p, sms, after_rows, s);
-    default: return chunk_dim<KV_NVFP4>(p, sms, after_rows, s);
+    case KV_BF16: return chunk_dim<KV_BF16>(p, sms, second, s);
+    case KV_Q8_0: return chunk_dim<KV_Q8_0>(p, sms, second, s);
+    case KV_FP8: return chunk_dim<KV_FP8>(p, sms, second, s);
+    default: return chunk_dim<KV_NVFP4>(p, sms, second, s);
   }
 }
 

@@ -456,7 +456,9 @@ size_t qmv_attn_workspace_size(const qmv_kv_cache* cache, int q_heads);
  * sequence's outputs are then unspecified, nothing else is touched. So does a batch of
  * more than 2^30 key tiles per SM (half a minute of work at least): none of it is computed. Table entries of
  * pages without a visible token are not followed (behind a window, they may be stale).
- * A batch that mixes single tokens and chunks launches two kernels, others one. Not
+ * Several sequences of which one may have a chunk (max_q above the few rows that stream
+ * the cache) launch two kernels, a call of one kind one; rows of no sequence do not change
+ * which. A max_q far above the batch's own only costs that second launch. Not
  * served: T * q_heads or max_pages * page_size of 2^31 and more, max_q rows per KV head or
  * max_pages * page_size / 16 * heads of 2^30 and more.
  * Sums, maxima and the output accumulate in fp32. Keys, values and queries enter the
