@@ -422,6 +422,7 @@ def qmv_gemv_int8dot(fmt, packed_W: torch.Tensor, x: torch.Tensor, N: int, K: in
 # These calls take single-digit microseconds on the device, so their checks are kept
 # lean: plain integers to ctypes, one stream look-up, one descriptor reference per cache.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _KV_TYPES = {torch.bfloat16: QMV_TYPE_BF16, torch.float32: QMV_TYPE_F32}
 
 
@@ -445,8 +446,18 @@ class KvCache:
         self.index, self.device = data.get_device(), data.device
         self.desc.data = data.data_ptr()
 
+    def _check_device(self) -> None:
+        """The library launches, and counts SMs, on the current device."""
+        if _current_device() != self.index:
+            raise ValueError(f"the cache is on device {self.index}, which is not the current device")
+
     def _stream(self, stream) -> int:
-        return _raw_stream(self.index) if stream is None else stream.cuda_stream
+        self._check_device()
+        if stream is None:
+            return _raw_stream(self.index)
+        if stream.device_index != self.index:
+            raise ValueError("stream must be on the cache's device")
+        return stream.cuda_stream
 
 
 def kv_cache(fmt, pages: int, page_size: int, heads: int, head_dim: int, k_scale: float = 1.0,
@@ -491,6 +502,7 @@ def qmv_kv_cache_size(cache: KvCache) -> int:
 
 
 def qmv_attn_workspace_size(cache: KvCache, q_heads: int) -> int:
+    cache._check_device()
     return int(_attn_ws(cache.ref, q_heads))
 
 

@@ -1,0 +1,59 @@
+"""The cache's and its attention's binding on a machine without a GPU: what it refuses before it
+calls the library. A stand-in cache on device -1, where CPU tensors are, passes the device
+checks of the tensors."""
+import ctypes
+import types
+
+import pytest
+import torch
+
+
+@pytest.fixture
+def q(monkeypatch):
+    import block_quantized_weight_fly_gb300 as q
+    monkeypatch.setattr(q, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(q, "_current_device", lambda: -1)
+    for name in ("_kv_write", "_kv_read", "_attn", "_attn_ws"):          # nothing reaches the library
+        monkeypatch.setattr(q, name, lambda *a: 0)
+    return q
+
+
+def stand_in(q):
+    c = q.KvCache.__new__(q.KvCache)
+    c.desc = q.KvDesc(1, 16, 2, 64, 4, 1.0, 1.0, 256)
+    c.ref = ctypes.byref(c.desc)
+    c.heads, c.head_dim, c.index, c.device = 2, 64, -1, torch.device("cpu")
+    c.data = torch.zeros(8, dtype=torch.uint8)
+    return c
+
+
+def calls(q, c, **kw):
+    x = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+    slots = torch.zeros(3, dtype=torch.int64)
+    a = dict(q=torch.zeros((3, 4, 64), dtype=torch.bfloat16), page_table=torch.zeros((1, 4), dtype=torch.int32),
+             kv_len=torch.zeros(1, dtype=torch.int32), q_start=torch.zeros(2, dtype=torch.int32), max_q=3,
+             ws=torch.zeros(64, dtype=torch.uint8))
+    a.update({k: v for k, v in kw.items() if k != "stream"})
+    s = {"stream": kw["stream"]} if "stream" in kw else {}
+    return [lambda: q.qmv_kv_write(c, x, x, slots, **s), lambda: q.qmv_kv_read(c, slots, **s),
+            lambda: q.qmv_attn_paged(c, **a, **s)]
+
+
+def test_the_stand_in_passes(q):
+    for call in calls(q, stand_in(q)):
+        call()
+
+
+def test_a_cache_that_is_not_on_the_current_device(q, monkeypatch):
+    c = stand_in(q)
+    monkeypatch.setattr(q, "_current_device", lambda: 0)
+    for call in calls(q, c) + [lambda: q.qmv_attn_workspace_size(c, 4)]:
+        with pytest.raises(ValueError, match="current device"):
+            call()
+
+
+def test_a_stream_of_another_device(q):
+    other = types.SimpleNamespace(device_index=1, cuda_stream=0)
+    for call in calls(q, stand_in(q), stream=other):
+        with pytest.raises(ValueError, match="stream"):
+            call()
