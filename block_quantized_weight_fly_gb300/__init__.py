@@ -103,6 +103,9 @@ EXPORTED = ["qmv_canon_size", "qmv_pack_size", "qmv_pack", "qmv_quantize", "qmv_
             "qmv_kv_cache_size", "qmv_kv_write", "qmv_kv_read", "qmv_attn_workspace_size", "qmv_attn_paged"]
 
 
+_current_device = torch._C._cuda_getDevice
+
+
 def _fmt(fmt) -> int:
     return FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
 
@@ -112,6 +115,8 @@ def _ptr(t: torch.Tensor | None):
         return None
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
+    if t.is_cuda and t.get_device() != _current_device():       # the library launches on the current device
+        raise ValueError(f"tensor on device {t.get_device()}, which is not the current device")
     return ctypes.c_void_p(t.data_ptr())
 
 
@@ -422,7 +427,6 @@ def qmv_gemv_int8dot(fmt, packed_W: torch.Tensor, x: torch.Tensor, N: int, K: in
 # These calls take single-digit microseconds on the device, so their checks are kept
 # lean: plain integers to ctypes, one stream look-up, one descriptor reference per cache.
 _raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
 _KV_TYPES = {torch.bfloat16: QMV_TYPE_BF16, torch.float32: QMV_TYPE_F32}
 
 
