@@ -165,11 +165,24 @@ def _act(x: torch.Tensor, K: int, rows: int | None = None) -> tuple[torch.Tensor
     return x, M
 
 
-def _out(y: torch.Tensor | None, shape, dev, name: str) -> torch.Tensor:
+def _empty(shape, dtype, dev, stream) -> torch.Tensor:
+    """Memory for an output, taken on the stream that will write it: the allocator may hand out a
+    block that earlier work of the stream it belongs to has yet to finish with. The current
+    stream, where the caller goes on, is noted as a user of it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _out(y: torch.Tensor | None, shape, dev, name: str, stream=None) -> torch.Tensor:
     """An fp32 output of `shape`: allocated if None, else checked (float32, contiguous,
     on x's device, at least as many values as the library writes)."""
     if y is None:
-        return torch.empty(shape, dtype=torch.float32, device=dev)
+        return _empty(shape, torch.float32, dev, stream)
     if not y.is_cuda or y.device != torch.device(dev):
         raise ValueError(f"{name} must be a CUDA tensor on {dev}")
     if y.dtype != torch.float32:
@@ -225,7 +238,7 @@ def qmv_pack(fmt, canon: torch.Tensor, N: int, K: int, E: int = 1, dst: torch.Te
     if canon.numel() * canon.element_size() < qmv_canon_size(fmt, N, K, E):
         raise ValueError("canon is shorter than qmv_canon_size")
     if dst is None:
-        dst = torch.empty(size, dtype=torch.uint8, device=canon.device)
+        dst = _empty(size, torch.uint8, canon.device, stream)
     elif not dst.is_cuda or not dst.is_contiguous() or dst.numel() * dst.element_size() < size:
         raise ValueError(f"dst must be a contiguous CUDA tensor of at least {size} bytes")
     _check(_pack(_fmt(fmt), _ptr(canon), N, K, E, _ptr(dst), _stream(stream)), "qmv_pack")
@@ -242,7 +255,7 @@ def qmv_quantize(fmt, W: torch.Tensor, tensor_scale: float = 0.0, canon: torch.T
     if not W.is_contiguous():
         raise ValueError("W must be contiguous")
     if canon is None:
-        canon = torch.empty(size, dtype=torch.uint8, device=W.device)
+        canon = _empty(size, torch.uint8, W.device, stream)
     elif not canon.is_cuda or not canon.is_contiguous() or canon.numel() * canon.element_size() < size:
         raise ValueError(f"canon must be a contiguous CUDA tensor of at least {size} bytes")
     _check(_quantize(_fmt(fmt), _ptr(W), rows, K, float(tensor_scale), _ptr(canon), _stream(stream)),
@@ -266,7 +279,7 @@ def qmv_quantize_codebook(fmt, W: torch.Tensor, codebook, canon: torch.Tensor | 
     rows, K = W.shape
     size = qmv_canon_size(fmt, rows, K, 1)
     if canon is None:
-        canon = torch.empty(size, dtype=torch.uint8, device=W.device)
+        canon = _empty(size, torch.uint8, W.device, stream)
     elif not canon.is_cuda or not canon.is_contiguous() or canon.numel() * canon.element_size() < size:
         raise ValueError(f"canon must be a contiguous CUDA tensor of at least {size} bytes")
     _check(_quantize_cb(_fmt(fmt), _ptr(W), rows, K, ctypes.cast(cb, ctypes.c_void_p), _ptr(canon),
@@ -278,7 +291,7 @@ def qmv_dequant(fmt, packed: torch.Tensor, N: int, K: int, E: int = 1, row0: int
                 rows: int | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     _dev(packed, "packed")
     rows = N * E - row0 if rows is None else rows
-    out = _out(out, (rows, K), packed.device, "out")
+    out = _out(out, (rows, K), packed.device, "out", stream)
     _check(_dequant(_fmt(fmt), _ptr(packed), N, K, E, row0, rows, _ptr(out), _stream(stream)),
            "qmv_dequant")
     return out
@@ -297,7 +310,7 @@ def qmv_gemv(fmt, packed_W: torch.Tensor, x: torch.Tensor, N: int, K: int,
              ws: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     _dev(packed_W, "packed_W"); _dev(x, "x"); _dev(ws, "ws")
     x, M = _act(x, K)
-    y = _out(y, (M, N), x.device, "y")
+    y = _out(y, (M, N), x.device, "y", stream)
     _check(_gemv(_fmt(fmt), _ptr(packed_W), _ptr(x), _ptr(y), M, N, K, _ptr(ws), ws.numel(),
                  _stream(stream)), "qmv_gemv")
     return y
@@ -308,7 +321,7 @@ def qmv_gemv_swiglu(fmt, tower: torch.Tensor, x: torch.Tensor, N: int, K: int, w
     """h = silu(gate . x) * (up . x) over a 2-expert tower (gate = expert 0, up = expert 1)."""
     _dev(tower, "tower"); _dev(x, "x"); _dev(ws, "ws")
     x, M = _act(x, K)
-    h = _out(h, (M, N), x.device, "h")
+    h = _out(h, (M, N), x.device, "h", stream)
     _check(_gemv_swiglu(_fmt(fmt), _ptr(tower), _ptr(x), _ptr(h), M, N, K, _ptr(ws), ws.numel(),
                         _stream(stream)), "qmv_gemv_swiglu")
     return h
@@ -320,7 +333,7 @@ def qmv_mlp_layer(fmt, gateup: torch.Tensor, down: torch.Tensor, x: torch.Tensor
     [N_ff, K_h] tower (gate, up), down = the [K_h, N_ff] matrix."""
     _dev(gateup, "gateup"); _dev(down, "down"); _dev(x, "x"); _dev(ws, "ws")
     x, M = _act(x, K_h)
-    y = _out(y, (M, K_h), x.device, "y")
+    y = _out(y, (M, K_h), x.device, "y", stream)
     _check(_mlp_layer(_fmt(fmt), _ptr(gateup), _ptr(down), _ptr(x), _ptr(y), M, N_ff, K_h, _ptr(ws), ws.numel(),
                       _stream(stream)), "qmv_mlp_layer")
     return y
@@ -332,7 +345,7 @@ def qmv_gemv_noalloc(fmt, packed_W: torch.Tensor, x: torch.Tensor, N: int, K: in
     required (the caller owns every buffer); nothing is allocated."""
     _dev(packed_W, "packed_W"); _dev(x, "x"); _dev(y, "y")
     x, M = _act(x, K)
-    y = _out(y, (M, N), x.device, "y")
+    y = _out(y, (M, N), x.device, "y", stream)
     _check(_gemv_noalloc(_fmt(fmt), _ptr(packed_W), _ptr(x), _ptr(y), M, N, K, _stream(stream)),
            "qmv_gemv_noalloc")
     return y
@@ -348,7 +361,7 @@ def qmv_grouped(fmt, tower: torch.Tensor, expert_ids: torch.Tensor, x: torch.Ten
         raise ValueError("expert_ids must be contiguous")
     M, topk = expert_ids.shape
     x, _ = _act(x, K, M * topk if x_per_pair else M)
-    y = _out(y, (M, topk, N), x.device, "y")
+    y = _out(y, (M, topk, N), x.device, "y", stream)
     _check(_grouped(_fmt(fmt), _ptr(tower), _ptr(expert_ids), _ptr(x), 1 if x_per_pair else 0, _ptr(y),
                     M, topk, N, K, E, _ptr(ws), ws.numel(), _stream(stream)), "qmv_grouped")
     return y
@@ -366,7 +379,7 @@ def qmv_grouped_swiglu(fmt, tower: torch.Tensor, expert_ids: torch.Tensor, x: to
         raise ValueError("expert_ids must be contiguous")
     M, topk = expert_ids.shape
     x, _ = _act(x, K, M)
-    h = _out(h, (M, topk, N), x.device, "h")
+    h = _out(h, (M, topk, N), x.device, "h", stream)
     _check(_grouped_swiglu(_fmt(fmt), _ptr(tower), _ptr(expert_ids), _ptr(x), _ptr(h), M, topk, N, K, E,
                            _ptr(ws), ws.numel(), _stream(stream)), "qmv_grouped_swiglu")
     return h
@@ -383,9 +396,9 @@ def qmv_quant_act_nvfp4(x: torch.Tensor, x_scale: float, codes: torch.Tensor | N
         if t is not None and (t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < n or not t.is_cuda):
             raise ValueError(f"{name} must be a contiguous CUDA uint8 tensor of at least {n} bytes")
     if codes is None:
-        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        codes = _empty((M, K // 2), torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty((M, K // 16), dtype=torch.uint8, device=x.device)
+        scales = _empty((M, K // 16), torch.uint8, x.device, stream)
     _check(_quant_act(_ptr(x), float(x_scale), _ptr(codes), _ptr(scales), M, K, _stream(stream)),
            "qmv_quant_act_nvfp4")
     return codes, scales
@@ -395,7 +408,7 @@ def qmv_gemm_nvfp4_w4a4(packed_W: torch.Tensor, x: torch.Tensor, x_scale: float,
                         ws: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     _dev(packed_W, "packed_W"); _dev(x, "x"); _dev(ws, "ws")
     x, M = _act(x, K)
-    y = _out(y, (M, N), x.device, "y")
+    y = _out(y, (M, N), x.device, "y", stream)
     _check(_w4a4(_ptr(packed_W), _ptr(x), float(x_scale), _ptr(y), M, N, K, _ptr(ws), ws.numel(),
                  _stream(stream)), "qmv_gemm_nvfp4_w4a4")
     return y
@@ -406,7 +419,7 @@ def qmv_gemm_kquant(fmt, packed_W: torch.Tensor, x: torch.Tensor, N: int, K: int
     """y = x . W^T for a K-quant W at prefill sizes (tensor cores, each weight read once)."""
     _dev(packed_W, "packed_W"); _dev(x, "x"); _dev(ws, "ws")
     x, M = _act(x, K)
-    y = _out(y, (M, N), x.device, "y")
+    y = _out(y, (M, N), x.device, "y", stream)
     _check(_kquant(_fmt(fmt), _ptr(packed_W), _ptr(x), _ptr(y), M, N, K, _ptr(ws), ws.numel(), _stream(stream)),
            "qmv_gemm_kquant")
     return y
@@ -417,7 +430,7 @@ def qmv_gemv_int8dot(fmt, packed_W: torch.Tensor, x: torch.Tensor, N: int, K: in
     """y = q8(x) . W^T: x quantized to int8 per 32 values, integer dots (Q8_0, Q4_K; M <= 8)."""
     _dev(packed_W, "packed_W"); _dev(x, "x"); _dev(ws, "ws")
     x, M = _act(x, K)
-    y = _out(y, (M, N), x.device, "y")
+    y = _out(y, (M, N), x.device, "y", stream)
     _check(_int8dot(_fmt(fmt), _ptr(packed_W), _ptr(x), _ptr(y), M, N, K, _ptr(ws), ws.numel(), _stream(stream)),
            "qmv_gemv_int8dot")
     return y
@@ -534,10 +547,10 @@ def qmv_kv_read(cache: KvCache, slots: torch.Tensor, dtype=torch.bfloat16, k: to
     pk = _index(k, shape, dtype, cache, "k") if k is not None else 0
     pv = _index(v, shape, dtype, cache, "v") if v is not None else 0
     if not pk:
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        k = _empty(shape, dtype, cache.device, stream)
         pk = k.data_ptr()
     if not pv:
-        v = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = _empty(shape, dtype, cache.device, stream)
         pv = v.data_ptr()
     st = _kv_read(cache.ref, ps, T, pk, pv, _KV_TYPES[dtype], cache._stream(stream))
     if st:
@@ -557,7 +570,7 @@ def qmv_attn_paged(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv
         raise ValueError(f"q must be a bfloat16 tensor [T, q_heads, {D}] on the cache's device")
     T, H, _ = q.shape
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=cache.device)
+        out = _empty((T, H, D), torch.bfloat16, cache.device, stream)
     elif out.dtype != torch.bfloat16 or out.shape != q.shape or out.get_device() != cache.index:
         raise ValueError("out must be bfloat16, of q's shape, on its device")
     qs, os = q.stride(), out.stride()

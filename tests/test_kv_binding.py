@@ -57,3 +57,28 @@ def test_a_stream_of_another_device(q):
     for call in calls(q, stand_in(q), stream=other):
         with pytest.raises(ValueError, match="stream"):
             call()
+
+
+def test_outputs_are_allocated_on_the_stream_that_writes_them(q, monkeypatch):
+    """... whose earlier work may not be done with a block of the current stream's."""
+    import contextlib
+    mine = types.SimpleNamespace(device_index=-1, cuda_stream=0)
+    on, took = [None], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        on.append(s)
+        yield
+        on.pop()
+
+    empty = torch.empty
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: (took.append(on[-1]), empty(*a, **kw))[1])
+    for call in calls(q, stand_in(q), stream=mine):
+        call()
+    assert took == [mine] * 3                                            # k, v and the attention's out
+    took.clear()
+    assert q._out(None, (2, 3), "cpu", "y", mine).shape == (2, 3) and took == [mine]
+    for call in calls(q, stand_in(q)):
+        call()
+    assert took[1:] == [None] * 3
