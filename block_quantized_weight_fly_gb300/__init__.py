@@ -579,8 +579,8 @@ def qmv_attn_paged(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
     B, P = page_table.shape
-    if ws.get_device() != cache.index:
-        raise ValueError("ws must be on the cache's device")
+    if ws.get_device() != cache.index or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous and on the cache's device")
     st = _attn(cache.ref, q.data_ptr(), qs[0], _index(page_table, (B, P), torch.int32, cache, "page_table"), P,
                _index(kv_len, (B,), torch.int32, cache, "kv_len"),
                _index(q_start, (B + 1,), torch.int32, cache, "q_start"), B, T, max_q, H,

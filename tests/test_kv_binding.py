@@ -82,3 +82,11 @@ def test_outputs_are_allocated_on_the_stream_that_writes_them(q, monkeypatch):
     for call in calls(q, stand_in(q)):
         call()
     assert took[1:] == [None] * 3
+
+
+def test_a_workspace_that_is_not_contiguous(q):
+    """numel() of an expanded or strided tensor says nothing about the memory behind it."""
+    c = stand_in(q)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 30), torch.zeros(64, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="ws"):
+            calls(q, c, ws=ws)[2]()
