@@ -9,6 +9,7 @@ the library has not been built, importing this package raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -443,13 +444,24 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _KV_TYPES = {torch.bfloat16: QMV_TYPE_BF16, torch.float32: QMV_TYPE_F32}
 
 
+def _int32(x, name: str) -> int:
+    """ctypes passes the low 32 bits of a larger number without a word."""
+    x = operator.index(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
 class KvCache:
     """One layer's paged cache: its device buffer (`data`, uint8) and its descriptor (`desc`)."""
 
     def __init__(self, fmt, pages: int, page_size: int, heads: int, head_dim: int, k_scale: float = 1.0,
                  v_scale: float = 1.0, device="cuda", data: torch.Tensor | None = None):
         f = KV_FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
-        self.desc = KvDesc(f, page_size, heads, head_dim, pages, k_scale, v_scale, None)
+        if not -(1 << 63) <= operator.index(pages) < 1 << 63:
+            raise ValueError(f"pages = {pages} does not fit 64 bits")
+        self.desc = KvDesc(_int32(f, "fmt"), _int32(page_size, "page_size"), _int32(heads, "heads"),
+                           _int32(head_dim, "head_dim"), pages, k_scale, v_scale, None)
         self.ref = ctypes.byref(self.desc)
         self.heads, self.head_dim = heads, head_dim
         size = qmv_kv_cache_size(self)
@@ -520,7 +532,7 @@ def qmv_kv_cache_size(cache: KvCache) -> int:
 
 def qmv_attn_workspace_size(cache: KvCache, q_heads: int) -> int:
     cache._check_device()
-    return int(_attn_ws(cache.ref, q_heads))
+    return int(_attn_ws(cache.ref, _int32(q_heads, "q_heads")))
 
 
 def qmv_kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
@@ -583,8 +595,8 @@ def qmv_attn_paged(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor, kv
         raise ValueError("ws must be contiguous and on the cache's device")
     st = _attn(cache.ref, q.data_ptr(), qs[0], _index(page_table, (B, P), torch.int32, cache, "page_table"), P,
                _index(kv_len, (B,), torch.int32, cache, "kv_len"),
-               _index(q_start, (B + 1,), torch.int32, cache, "q_start"), B, T, max_q, H,
-               D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(), os[0],
+               _index(q_start, (B + 1,), torch.int32, cache, "q_start"), B, T, _int32(max_q, "max_q"), H,
+               D ** -0.5 if scale is None else scale, 1 if causal else 0, _int32(window, "window"), out.data_ptr(), os[0],
                None if lse is None else _index(lse, (T, H), torch.float32, cache, "lse"), ws.data_ptr(),
                ws.numel() * ws.element_size(), cache._stream(stream))
     if st:

@@ -90,3 +90,19 @@ def test_a_workspace_that_is_not_contiguous(q):
     for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 30), torch.zeros(64, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError, match="ws"):
             calls(q, c, ws=ws)[2]()
+
+
+def test_integers_that_do_not_fit(q):
+    """2^32 + 5 is not 5."""
+    c = stand_in(q)
+    for name in ("max_q", "window"):
+        for value in ((1 << 32) + 5, 1 << 31, -(1 << 31) - 1):
+            with pytest.raises(ValueError, match=name):
+                calls(q, c, **{name: value})[2]()
+    with pytest.raises(ValueError, match="q_heads"):
+        q.qmv_attn_workspace_size(c, (1 << 32) + 4)
+    good = dict(pages=4, page_size=16, heads=2, head_dim=64)
+    for name, value in (("page_size", (1 << 32) + 16), ("heads", (1 << 32) + 2), ("head_dim", (1 << 32) + 64),
+                        ("pages", (1 << 64) + 4)):
+        with pytest.raises(ValueError, match=name):
+            q.KvCache("bf16", **{**good, name: value})
