@@ -905,10 +905,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
         float m = -INFINITY, l = 0.0f;
         bool bad_row = false;
         // S tiles e0 .. e1-1 are seen whole by every row and run the short form; the
-        // others, the two behind a cut tile (whose marks they look at) and the last one run
+        // others, the two behind a cut key tile (whose marks they look at, those of a half that
+        // is not cut itself among them: values are cleaned by key tiles) and the last one run
         // the long one
         const int key0 = (u.tile0 + u.k) * KT;                  // first key of the part
-        int e0 = full.lo > key0 ? (full.lo - key0 + kSub - 1) / kSub + 2 : 0;
+        int e0 = full.lo > key0 ? (full.lo - key0 + KT - 1) / KT * (KT / kSub) + 2 : 0;
         if (e0 > ns) e0 = ns;
         int e1 = full.hi + 1 - key0 >= 0 ? (full.hi + 1 - key0) / kSub : 0;
         if (e1 > ns - 1) e1 = ns - 1;
@@ -917,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
         // last two at the end.
         auto marks = [&](int j) {
           const int j0 = key0 + j * kSub;
-          if (!full.edge(j0, kSub)) return;
+          if (!full.edge(j0 / KT * KT, KT)) return;
           const uint32_t* bits = KT == kSub ? s_poison[(tileno + j) & 7] : &s_poison[(tileno + (j >> 1)) & 7][2 * (j & 1)];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
