@@ -474,7 +474,7 @@ qmv_status kv_geometry(const qmv_kv_cache* d, KvCache* c) {
   if (d->heads > 65536 || d->pages > ((int64_t)1 << 31) - 1) return QMV_EUNSUPPORTED;
   c->k_scale = c->v_scale = 1.0f;
   if (d->fmt == QMV_KV_FP8 || d->fmt == QMV_KV_NVFP4) {
-    const float top = 3.0e38f;
+    const float top = d->fmt == QMV_KV_NVFP4 ? 5.65e37f : 3.0e38f;     // 6 s is a divisor of NVFP4's
     if (!(d->k_scale > 0.0f && d->k_scale < top && d->v_scale > 0.0f && d->v_scale < top)) return QMV_EINVAL;
     c->k_scale = d->k_scale;
     c->v_scale = d->v_scale;

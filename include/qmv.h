@@ -392,7 +392,7 @@ typedef enum {
  * values, less than 2^48 bytes in all. page_size: a power of two, 16 .. 1024. head_dim: 64,
  * 128 or 256. heads: up to 65536. pages: below 2^31. data: device,
  * qmv_kv_cache_size bytes, 256-byte aligned, owned by the caller; it needs no
- * initial value. k_scale, v_scale: the static scales of FP8 and NVFP4 (finite, > 0; the
+ * initial value. k_scale, v_scale: the static scales of FP8 and NVFP4 (> 0, below 3e38, NVFP4 5.65e37; the
  * other formats ignore them). The layout is the library's own (qmv_kv_read gives the
  * values back); a page's bytes are contiguous, page_size * heads * (K + V row bytes), so
  * pages can be copied or swapped whole. */

@@ -28,3 +28,11 @@ def test_sizes_past_63_bits_are_refused(q, fmt, dim):
             assert q._kv_read(ctypes.byref(c), P, 4, P, P, 1, None) == 3
             assert q._kv_write(ctypes.byref(c), P, P, 1, 128, 64, 128, 64, P, 4, None) == 3
             assert q._attn_ws(ctypes.byref(c), 65536) == 0
+
+
+def test_nvfp4_scales_whose_six_fold_leaves_fp32_are_refused(q):
+    """b = amax / (6 s): with 6 s = inf every block would be stored as zeros."""
+    for s, served in ((5.6e37, True), (5.7e37, False), (1e38, False), (2.9e38, False)):
+        for kw in (dict(ks=s), dict(vs=s)):
+            assert (q._kv_size(ctypes.byref(desc(q, fmt=4, **kw))) > 0) == served, (s, kw)
+            assert q._kv_size(ctypes.byref(desc(q, fmt=3, **kw))) > 0
