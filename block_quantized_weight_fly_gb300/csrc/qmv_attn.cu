@@ -1,8 +1,10 @@
 // qmv_attn.cu -- attention of few new tokens over the paged KV cache: at most 16 query rows
 // per (sequence, KV head), 32 where registers allow (most_rows), a row being one query head
 // of one new token. Bound by the cache's bytes, each read once: 64 sequences of 200 to 16000
-// FP8 tokens (8 heads of 128) take 182 to 185 us, 6.1 TB/s; one of 262144 NVFP4 tokens 75 us, 5.4 TB/s
-// between its start and its joins, where the decoding instructions are what bounds it.
+// FP8 tokens (8 heads of 128) take 180 to 183 us, 6.2 TB/s; one of 262144 NVFP4 tokens 75 us, 4.0
+// TB/s, with no unit full: DRAM at half its rate, issue slots 51 % (59 % of the active cycles), tensor
+// pipe 17 %. Its 16 warps are held to 128 registers each, spill 106 bytes of stores and 132 of
+// loads, and stall on fixed latencies, on one another and on the math pipe before memory.
 //
 // Work: the cached tokens of every (sequence, KV head) in tiles of 32 (wide rows: 16),
 // numbered through; each CTA takes one contiguous range of tiles, whatever the lengths are
@@ -923,7 +925,12 @@ cudaError_t rows_fmt(const RowsParams& p, int sms, bool second, cudaStream_t s) 
 // 16 and 32 rows | chunk kernel: D = 64: FP8 98, 147 | 195, BF16 111, 155 | 194, NVFP4 102, 154
 // | 201, Q8_0 109, 163 | 202. D = 128: NVFP4 137, 247 | 353; FP8 125, 238 | 230, BF16 195, 281 |
 // 226, Q8_0 141, 272 | 268. D = 256, where O of 32 rows does not fit a warp's registers: Q8_0
-// 249 | 360.
+// 249 | 360. The 32-row form wins at every other shape tried too, 32 rows of it against 33 of the
+// chunk kernel: one sequence of 131072 tokens, 8 heads and 1: FP8 D = 64 78, 68 | 121, 134, NVFP4
+// D = 128 126, 111 | 195, 179; 32 of 16000, 1 head: 52 | 81, 76 | 117; 128 of 500, 4 heads: 58 |
+// 85, 78 | 115; 4 of 333, 8 heads: 19 | 46, 21 | 56. The 16-row form is ahead of or even with
+// the chunk kernel's 17 rows at all of these in every format and width (BF16 D = 256, one of 131072: 207 |
+// 207). Not tried at them: a 32-row form of the other three formats with D = 128.
 static int most_rows(const KvCache& c) { return c.dim == 64 || (c.dim == 128 && c.fmt == KV_NVFP4) ? 32 : 16; }
 
 // counters, then two parts of most_rows rows per CTA
@@ -944,7 +951,7 @@ cudaError_t launch_attn_rows(const AttnArgs& a, int sms, bool second, cudaStream
 // Sequences with few query rows per KV head are bound by the cache's bytes and go to the
 // streaming kernel, the others to the tensor-core kernel with its tiles of 128 rows. A batch
 // of single tokens and one chunk takes both: 47 single tokens and a chunk of 777 took 407 us
-// in 128-row tiles alone, 171 to 176 us split.
+// in 128-row tiles alone, 171 to 173 us split.
 cudaError_t launch_attn(AttnArgs a, cudaStream_t s) {
   const int sms = num_sms_current_device();
   if (sms <= 0) return cudaErrorInvalidDevice;

@@ -21,9 +21,11 @@
 // runs under the softmax of these; two row tiles of 128 (D <= 128; O of D = 256 fills
 // half of tensor memory) share each key and value tile. P takes the place of its S.
 // Bound by the tensor cores and, behind them, by the softmax's latency per 64 keys: 2048
-// tokens of 64 heads after 28001 FP8 ones (D = 128) take 1356 to 1380 us, 1.42 PFLOP/s; fresh BF16
-// prompts of 700 to 6001 tokens 781 to 791 us, 1.07 PFLOP/s (half of the last tiles is masked); 8 new
-// tokens of 24 heads (D = 256, 48 of 128 rows used) over 15000 Q8_0 ones, five times, 91 to 94 us.
+// tokens of 64 heads after 28001 FP8 ones (D = 128) take 1363 to 1387 us, 1.42 PFLOP/s; fresh BF16
+// prompts of 700 to 6001 tokens 800 us, 1.06 PFLOP/s (half of the last tiles is masked); 8 new
+// tokens of 24 heads (D = 256, 48 of 128 rows used) over 15000 Q8_0 ones, five times, 96 us.
+// All twelve instances spill 336 to 548 bytes of stores at the launch's 128 registers (the roles'
+// shares, which setmaxnreg gives them, change nothing in the code).
 #include <type_traits>
 #include "qmv_attn.cuh"
 
@@ -301,7 +303,7 @@ __device__ __forceinline__ bool clean8(uint32_t* o) {
 // One part (keys or values) of a tile, codes -> operand rows; warp cw of TEAM. The loads of
 // a batch come before its stores: the two may alias as far as the compiler knows, and
 // piece by piece each load waited for the stores before it (1500 cycles per part, against
-// 500). EDGE: values that are not finite are taken out, their tokens marked.
+// 620). EDGE: values that are not finite are taken out, their tokens marked.
 template <int FMT, int D, bool EDGE>
 __device__ __forceinline__ void convert_part(const uint8_t* raw, uint8_t* op, uint32_t* poison, int cw, int lane) {
   using C = ChunkCfg<FMT, D>;

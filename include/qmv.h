@@ -443,8 +443,8 @@ size_t qmv_attn_workspace_size(const qmv_kv_cache* cache, int q_heads);
  * over the visible keys: causal != 0: j <= p; window > 0 (with causal only): also
  * j > p - window; causal == 0: all n. A query that sees none (n = 0, or p < 0 when c > n)
  * gets o = 0, lse = -inf. What is not visible counts for nothing, whatever it holds; a
- * visible value row that is not finite makes NaN of the outputs that see it (all of a
- * query's head_dim outputs, or only the affected ones).
+ * visible value row that is not finite makes NaN, or for an infinity an infinity or NaN,
+ * of the outputs that see it (all of a query's head_dim outputs, or only the affected ones).
  * q, out: device bf16 [T][q_heads][head_dim], rows of head_dim contiguous values, tokens
  * q_token_stride / out_token_stride values apart, heads head_dim apart; 16-byte aligned,
  * strides a multiple of 8. lse: device fp32 [T][q_heads], or null. page_table: device
@@ -454,15 +454,17 @@ size_t qmv_attn_workspace_size(const qmv_kv_cache* cache, int q_heads);
  * picks the kernel. A kv_len outside 0 .. max_pages * page_size, a c above max_q, a
  * q_start out of order or a page id outside the cache latches QMV_ERANGE; the
  * sequence's outputs are then unspecified, nothing else is touched. So does a batch of
- * more than 2^30 key tiles per SM (half a minute of work at least): none of it is computed. Table entries of
- * pages without a visible token are not followed (behind a window, they may be stale).
- * Several sequences of which one may have a chunk (max_q above the few rows that stream
- * the cache) launch two kernels, a call of one kind one; rows of no sequence do not change
- * which. A max_q far above the batch's own only costs that second launch. Not
- * served: T * q_heads or max_pages * page_size of 2^31 and more, max_q rows per KV head or
- * max_pages * page_size / 16 * heads of 2^30 and more.
+ * more than 2^30 key tiles per SM (half a minute of work at least): none of it is computed.
+ * Table entries of pages without a visible token are not followed (behind a window, they
+ * may be stale). Where max_q allows a sequence more rows than stream the cache, several
+ * sequences launch two kernels and each takes its own, whatever rows of no sequence there
+ * are; a single one is taken to be a chunk if T >= max_q. Not served: T * q_heads or
+ * max_pages * page_size of 2^31 and more, max_q rows per KV head or max_pages * page_size /
+ * 16 * heads of 2^30 and more.
  * Sums, maxima and the output accumulate in fp32. Keys, values and queries enter the
- * products exactly, Q8_0 ones as f16(d q); probabilities are rounded to 16
+ * products exactly, but for Q8_0 keys and values, which do as f16(d q), and, unless the
+ * cache is BF16, query values below 2^-28 of their row's largest, which f16's smallest
+ * step may round (by up to 2^-39 of the largest); probabilities are rounded to 16
  * bits before they meet the values: for a BF16 cache to bf16 (2^-8 of each), else to f16
  * (2^-11 of each; one below 2^-21 of its row's largest, by up to 2^-32 of the largest). */
 qmv_status qmv_attn_paged(const qmv_kv_cache* cache, const uint16_t* q, int64_t q_token_stride,
